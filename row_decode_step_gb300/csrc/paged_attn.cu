@@ -274,7 +274,8 @@ __device__ __forceinline__ void join_parts(Part part, int n, int nq, float *s_w,
             const float r = __ldcg(part(i) + QT * D + qi), l = __ldcg(part(i) + QT * D + QT + qi);
             s_w[i * QT + qi] = r;
             const float m = fmaxf(R, r);
-            if (m != -INFINITY) L = L * exp2_approx(R - m) + l * exp2_approx(r - m);
+            // (no reference yet: the sums are 0, or the NaN of a query that is none)
+            L = m == -INFINITY ? L + l : L * exp2_approx(R - m) + l * exp2_approx(r - m);
             R = m;
         }
         float m = R;
