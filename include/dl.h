@@ -736,7 +736,8 @@ int dl_paged_attn_workspace_size(int n_q, int n_kv, int head_dim, size_t *bytes)
  *             sequence only) row r's KV head h reads, of its P pages, the first
  *             min(P, n_list) listed: indexes into its table row (as dl_paged_select writes)
  *   out       device f32, row r at out + r*out_stride, apart from q; a row that sees no key gets 0
- *   lse       device f32 [rows][n_q] or NULL; -inf for a row that sees no key
+ *   lse       device f32 [rows][n_q] or NULL; -inf for a row that sees no key.  A query that is not
+ *             finite, or whose largest score passes f32, is NaN in both
  *   workspace device, dl_paged_attn_workspace_size bytes, 16-byte aligned, zero before its
  *             first use; every call leaves its counters zero.  Two calls whose kernels
  *             may overlap on the GPU need a workspace each

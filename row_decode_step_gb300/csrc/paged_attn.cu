@@ -199,6 +199,8 @@ __device__ __forceinline__ float scale_of(const uint32_t *w, int b)
     return b & 1 ? __high2float(h) : __low2float(h);
 }
 
+constexpr float kFar = 4194304.f;            // 2^22
+
 constexpr int kDesc = 32;                    // chunks of a warp that are described at a time, in two halves
 
 // Shared memory: the warps' rings, the warps' outputs (whose room the references of an item's parts take
@@ -587,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(qv[b][i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // power of two that brings the largest |q| into [2^14, 2^15)
-        const int e = min(100, max(-90, 14 - ((int)(__float_as_uint(top) >> 23) - 127)));
+        // power of two that brings the largest |q| into [2^14, 2^15) (-113: that of the largest number)
+        const int e = min(100, max(-113, 14 - ((int)(__float_as_uint(top) >> 23) - 127)));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         const float back = a.qk_scale * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
         uint32_t dtop = 0;                   // largest V scale so far (f16 bits)
         float kshift = 0.f;                  // P carries 2^kshift and d 2^dshift: together they put P d
         int dshift = 0;                      // under 2^15
-        bool started = false;                // every query of the tile has seen a key
+        bool started = false;                // every query of the tile has seen a key, none a far one
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
         mraw[0] = mraw[1] = -INFINITY;
@@ -709,12 +711,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
             // tile has seen a key
             float most = -INFINITY;
             const float2 minus = make_float2(-ref.x, -ref.y);
+            float2 ex[2][2];                 // the exponents
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 x = __ffma2_rn(sc[t][i], cq, minus);
-                    most = fmaxf(most, fmaxf(x.x, x.y));
+                    ex[t][i] = __ffma2_rn(sc[t][i], cq, minus);
+                    most = fmaxf(most, fmaxf(ex[t][i].x, ex[t][i].y));
                 }
             const bool stale = most > kshift + 1.f || dmine > dtop || !started;
             if (__any_sync(0xffffffffu, stale)) {
@@ -739,8 +742,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
                 mraw[0] = fmaxf(mx, mraw[0]);
                 mraw[1] = fmaxf(my, mraw[1]);
                 seen = seen && mraw[0] != -INFINITY && mraw[1] != -INFINITY;
-                const float2 nref = make_float2(mraw[0] == -INFINITY ? 0.f : fmaf(mraw[0], cq.x, -kshift),
-                                                mraw[1] == -INFINITY ? 0.f : fmaf(mraw[1], cq.y, -kshift));
+                float2 nref = make_float2(mraw[0] == -INFINITY ? 0.f : fmaf(mraw[0], cq.x, -kshift),
+                                          mraw[1] == -INFINITY ? 0.f : fmaf(mraw[1], cq.y, -kshift));
+                // References as large as this are off by a quarter of an exponent and more, so that the products'
+                // exact differences from them are nobody's weights (past f16 from 2^25 on): here the scores are
+                // rounded first and the largest weight is 1, chunk by chunk.
+                const bool far_x = fabsf(nref.x) >= kFar, far_y = fabsf(nref.y) >= kFar;
+                if (far_x) nref.x = __fmul_rn(mraw[0], cq.x);
+                if (far_y) nref.y = __fmul_rn(mraw[1], cq.y);
+                seen = seen && !far_x && !far_y;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ex[t][i].x = far_x ? __fsub_rn(__fmul_rn(sc[t][i].x, cq.x), nref.x) : fmaf(sc[t][i].x, cq.x, -nref.x);
+                        ex[t][i].y = far_y ? __fsub_rn(__fmul_rn(sc[t][i].y, cq.y), nref.y) : fmaf(sc[t][i].y, cq.y, -nref.y);
+                    }
                 // (a query that has seen nothing has sums of zero: any finite factor will do)
                 const float2 f = make_float2(exp2_approx(fminf(ref.x - nref.x, 100.f)),
                                              exp2_approx(fminf(ref.y - nref.y, 100.f)));
@@ -772,8 +789,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 e = __ffma2_rn(sc[t][i], cq, make_float2(-ref.x, -ref.y));
-                    const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    const float2 w = make_float2(exp2_approx(ex[t][i].x), exp2_approx(ex[t][i].y));
                     sum = __fadd2_rn(sum, w);
                     uint32_t hi, lo;
                     split2(w.x, w.y, hi, lo);

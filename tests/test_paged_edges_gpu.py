@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged
-from tests.test_paged_gpu import _cuda, _pool, _tables
+from tests.test_paged_gpu import _check, _cuda, _pool, _tables
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,43 @@ def test_odd_queries_of_cut_items(dl, D, n_q, n_kv):
     assert np.isnan(ls[bad]).all(), ls[bad]
     ok = np.abs(o - want[0].reshape(4, n_q, D)) <= want[2].reshape(4, n_q, D)
     assert ok[~bad].all() and (np.abs(ls - want[1]) <= want[3])[~bad].all()
+
+
+@pytest.mark.parametrize("D,n_q,n_kv", [(128, 8, 2), (64, 16, 2)])
+@pytest.mark.parametrize("scale,qscale", [(1.0, 1e4), (1.0, 1e5), (1.0, 1e6), (1.0, 1e7), (1.0, 1e12), (1.0, 1e33), (1e-3, 1e40),
+                                          (300.0, 1e3)])
+def test_large_scores(dl, D, n_q, n_kv, scale, qscale):
+    """Scores up to f32's range.  Each query is a key of its sequence times `qscale`, which beats every other key by far
+    more than a score's error, so that the weights are 1 and 0; in the second sequence all pages hold the same keys and
+    values of their own, whose scores are equal bit for bit.  The bound is the attention's without the error of scores."""
+    rng = np.random.default_rng(int(np.log10(qscale)) + D)
+    page, lens, G = 32, [3000, 40 * 32, 1, 40], n_q // n_kv
+    tables, n_pages = _tables(rng, lens, page)
+    pool, _ = _pool(rng, n_pages, n_kv, page, D, scale)
+    pool[tables[1, 1:40], ..., :9 * D] = pool[tables[1, 0], ..., :9 * D]
+    K, V = paged.keys_values(pool, D)
+    q = np.zeros((4, n_q, D), np.float32)
+    for s, n in enumerate(lens):
+        for h in range(n_q):
+            t = int(rng.integers(0, n))
+            q[s, h] = K[tables[s, t // page], h // G, t % page] * qscale
+    assert np.isfinite(q).all()
+    kw = dict(n_q=n_q, n_kv=n_kv, D=D, page=page)
+    q = q.reshape(4, -1)
+    lbound = paged.attention(q, pool, tables, lens, **kw)[3]        # (2^-21 (1 + |lse|) and a score's error)
+    out, bound, lse = np.zeros((4, n_q, D)), np.zeros((4, n_q, D)), np.zeros((4, n_q))
+    for s, n in enumerate(lens):
+        for h in range(n_q):
+            at = np.arange(n)
+            k, v = (x[tables[s, at // page], h // G, at % page] for x in (K, V))
+            sc = (k * q[s].reshape(n_q, D)[h].astype(np.float64)).sum(-1) / np.sqrt(D)
+            top = (k == k[sc.argmax()]).all(-1)
+            if not top.all():
+                assert (sc.max() - sc[~top]).min() > 2 * lbound[s, h] + 100
+            out[s, h], lse[s, h] = v[top].mean(0), sc.max() + np.log(top.sum())
+            bound[s, h] = (2.0 ** -19 + n / 16 * 2.0 ** -23) * np.abs(v[top]).mean(0) + \
+                (n * 2.0 ** -32 + 2.0 ** -29) * np.abs(v).max()
+    gp, gq, gt, gl = _cuda(pool, q, tables, np.array(lens, np.int32))
+    ls = torch.empty(4, n_q, device="cuda")
+    got = dl.dl_paged_attn(gq, dl.PagedKV(gp, page, D), gt, gl, dl.paged_attn_workspace(n_q, n_kv, D), n_q, None, ls)
+    _check(got.cpu().numpy(), ls.cpu().numpy(), (out.reshape(4, -1), lse, bound.reshape(4, -1), lbound))
