@@ -26,7 +26,6 @@
 //
 // Bound by a warp's own chain of instructions (730 for 32 keys, 0.6 a cycle and scheduler): 16 sequences
 // of 32768 keys run at 4.5 TB/s (134 us), with the codes used undecoded (wrong, to see) at 5.3.
-#include <atomic>
 #include <cmath>
 
 #include "dl_async.cuh"
@@ -970,25 +969,14 @@ int launch(PagedAttnArgs &a, int sms, int64_t most_chunks, unsigned char *worksp
     // the references of a group's parts lie where the warps' outputs did
     if ((int64_t)(group_size_most(full) + 1) * QT * 4 > out_bytes(D, QT))
         return dl::fail(DL_E_SHAPE, "dl_paged_attn: %d CTAs are more parts than an item's join holds", full);
-    // Past the default limit (48 KB with the kernel's 7 KB of static shared memory) the kernel asks for its
-    // shared memory once a device; a launch that finds the limit unset all the same (after a reset of the
-    // device) asks and launches again.
+    auto go = [&]() {
+        return dl::launch_pdl(paged_attn_kernel<D, QT>, dim3((unsigned)grid), dim3(kThreads), smem, st,
+                              "dl_paged_attn: launch", a);
+    };
+    if constexpr (smem <= 41 * 1024) return go();        // (48 KB with the kernel's 7 KB of static shared memory)
     static std::atomic<uint64_t> asked{0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    for (bool ask = smem > 41 * 1024 && !(asked.load() & bit);; ask = true) {
-        if (ask) {
-            cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return dl::cuda_fail(e, "dl_paged_attn: shared memory");
-            asked |= bit;
-        }
-        const int rc = dl::launch_pdl(paged_attn_kernel<D, QT>, dim3((unsigned)grid), dim3(kThreads), smem, st,
-                                      "dl_paged_attn: launch", a);
-        if (rc == DL_OK || ask || smem <= 41 * 1024) return rc;
-        cudaGetLastError();
-        dl::clear_error();
-    }
+    return dlp::launch_wide(reinterpret_cast<const void *>(paged_attn_kernel<D, QT>), smem, asked,
+                            "dl_paged_attn: shared memory", go);
 }
 
 int check_heads(const char *who, int n_q, int n_kv, int D)

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "dl_common.cuh"
@@ -32,6 +33,29 @@ __host__ __device__ constexpr int v_half_off(int D, int s, int d)
 }
 
 inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128 || page == 256; }
+
+// A launch whose dynamic shared memory passes the default limit: the kernel asks once a device for `most`, the
+// largest of its launches, and never for less, since the limit is one for all host threads.  A launch that finds
+// it unset all the same (after a reset of the device) asks and launches again.  `asked`: of this kernel, a bit
+// a device.
+template <typename Launch>
+int launch_wide(const void *kern, int most, std::atomic<uint64_t> &asked, const char *who, Launch launch)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    for (bool ask = !(asked.load() & bit);; ask = true) {
+        if (ask) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            if (e != cudaSuccess) return dl::cuda_fail(e, who);
+            asked |= bit;
+        }
+        const int rc = launch();
+        if (rc == DL_OK || ask) return rc;
+        cudaGetLastError();
+        dl::clear_error();
+    }
+}
 
 // Checks of a cache and its tables that every call makes; DL_OK or the recorded failure.
 int check_cache(const char *who, const dl_paged_kv *kv, const dl_block_tables *t, int n_q, bool want_mean);

@@ -341,6 +341,34 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) paged_select_kernel(
     for (int i = lo + take + np - hi + tid; i < cap; i += kThreads) dst[i] = -1;
 }
 
+constexpr int smem_bytes(int width) { return width * 4 + 3 * kBins * 4; }
+
+template <int D, int kThreads>
+int launch(const SelectArgs &a, int rows, int C, cudaStream_t st)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)C, (unsigned)rows, (unsigned)a.n_kv);
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = (size_t)smem_bytes(a.width);
+    lc.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = C > 1 ? 2 : 1;
+    auto go = [&]() {
+        cudaError_t e = cudaLaunchKernelEx(&lc, paged_select_kernel<D, kThreads>, a);
+        return e == cudaSuccess ? DL_OK : dl::cuda_fail(e, "dl_paged_select: launch");
+    };
+    if (smem_bytes(a.width) <= 40 * 1024) return go();   // (the default limit is 48 KB with the static part)
+    static std::atomic<uint64_t> asked{0};
+    return dlp::launch_wide(reinterpret_cast<const void *>(paged_select_kernel<D, kThreads>),
+                            smem_bytes(DL_PAGED_MAX_WIDTH), asked, "dl_paged_select: shared memory", go);
+}
+
 }  // namespace
 
 extern "C" {
@@ -378,30 +406,9 @@ int dl_paged_select(const float *q, int64_t q_stride, const dl_paged_kv *kv, con
     int C = 1;
     while (C < 8 && (int64_t)rows * kv->n_kv * C * 2 <= 3 * (int64_t)sms && tables->width >= C * 2 * 64) C *= 2;
     const int threads = (int64_t)rows * kv->n_kv * C <= sms ? 512 : 256;
-    void (*kern)(SelectArgs) = kv->head_dim == 128
-                                   ? (threads == 512 ? paged_select_kernel<128, 512> : paged_select_kernel<128, 256>)
-                                   : (threads == 512 ? paged_select_kernel<64, 512> : paged_select_kernel<64, 256>);
-    const size_t smem = (size_t)tables->width * 4 + 3 * kBins * 4;
-    if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return dl::cuda_fail(e, "dl_paged_select: shared memory");
-    }
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)C, (unsigned)rows, (unsigned)kv->n_kv);
-    lc.blockDim = dim3((unsigned)threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    lc.attrs = attr;
-    lc.numAttrs = C > 1 ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&lc, kern, a);
-    if (e != cudaSuccess) return dl::cuda_fail(e, "dl_paged_select: launch");
-    return DL_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (kv->head_dim == 128) return threads == 512 ? launch<128, 512>(a, rows, C, st) : launch<128, 256>(a, rows, C, st);
+    return threads == 512 ? launch<64, 512>(a, rows, C, st) : launch<64, 256>(a, rows, C, st);
 }
 
 }  // extern "C"

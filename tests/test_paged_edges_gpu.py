@@ -1,4 +1,7 @@
 """Calls of the paged 4-bit cache at the edges of what their documentation allows."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -80,3 +83,41 @@ def test_large_scores(dl, D, n_q, n_kv, scale, qscale):
     ls = torch.empty(4, n_q, device="cuda")
     got = dl.dl_paged_attn(gq, dl.PagedKV(gp, page, D), gt, gl, dl.paged_attn_workspace(n_q, n_kv, D), n_q, None, ls)
     _check(got.cpu().numpy(), ls.cpu().numpy(), (out.reshape(4, -1), lse, bound.reshape(4, -1), lbound))
+
+
+def test_select_from_two_threads(dl):
+    """Tables of different widths, each past the default limit of shared memory, from two host threads at once (the C
+    calls, which ctypes makes without the interpreter's lock)."""
+    D, page, n_kv, n_q = 64, 16, 1, 4
+    rng = np.random.default_rng(3)
+    runs = []
+    for width in (16384, 5000):                         # the most there may be, and a few more than 4096
+        mean = rng.standard_normal((64, n_kv, D)).astype(np.float16)
+        tables = rng.integers(0, 64, (1, width)).astype(np.int32)
+        q = rng.standard_normal((1, n_q * D)).astype(np.float32)
+        lens = [width * page]
+        want = paged.select(q, mean, tables, lens, n_q=n_q, n_kv=n_kv, D=D, page=page, top_k=5, sink=1, local=2)
+        gm, gt, gq, gl = _cuda(mean, tables, q, np.array(lens, np.int32))
+        kv = dl.PagedKV(dl.PagedKV.empty(64, n_kv, page, D).pool, page, D, k_mean=gm)
+        pages, stream = torch.zeros(1, n_kv, 8, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+        c = dl.dl_block_tables(gt.data_ptr(), width, 1, width)
+        ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        args = (ptr(gq), n_q * D, ctypes.byref(kv.c), ctypes.byref(c), ptr(gl), 1, n_q, 5, 1, 2, ptr(pages), None,
+                ctypes.c_void_p(stream.cuda_stream))
+        runs.append((args, pages, want, (gm, gt, gq, gl, kv, c, stream)))
+    torch.cuda.synchronize()
+    refused, ready = [], threading.Barrier(2)
+
+    def work(args):
+        ready.wait(timeout=60)
+        refused.append(sum(dl.lib().dl_paged_select(*args) != dl.DL_OK for _ in range(3000)))
+
+    threads = [threading.Thread(target=work, args=r[:1]) for r in runs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0, 0]
+    for _, pages, want, _ in runs:
+        assert np.array_equal(pages.cpu().numpy(), want)
