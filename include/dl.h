@@ -739,8 +739,9 @@ int dl_paged_attn_workspace_size(int n_q, int n_kv, int head_dim, size_t *bytes)
  *   lse       device f32 [rows][n_q] or NULL; -inf for a row that sees no key.  A query that is not
  *             finite, or whose largest score passes f32, is NaN in both
  *   workspace device, dl_paged_attn_workspace_size bytes, 16-byte aligned, zero before its
- *             first use; every call leaves its counters zero.  Two calls whose kernels
- *             may overlap on the GPU need a workspace each
+ *             first use; every call leaves its counters zero.  Calls of any rows and heads
+ *             may take turns on one; two calls whose kernels may overlap on the GPU need
+ *             a workspace each
  *   status    device int32 or NULL: DL_STATUS_SEQLEN_RANGE; DL_STATUS_PAGE_RANGE where a page outside
  *             the pool (or listed outside the sequence) is met, whose keys are then left out
  * Errors: DL_E_SHAPE (n_q no multiple of n_kv, more than 16 heads to a KV head, ...),

@@ -36,7 +36,7 @@ def nvcc() -> str:
 
 
 def _deps() -> list:
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "dl.h")]
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "dl.h")]
 
 
 def _stale(target: str, sources: list) -> bool:

@@ -30,6 +30,7 @@
 
 #include "dl_async.cuh"
 #include "paged_kv.cuh"
+#include "paged_layout.h"
 
 namespace {
 
@@ -45,11 +46,8 @@ constexpr int kKept = 512;                   // sequences whose lengths a CTA co
                                              // (256 short sequences: 20.0 us, after the wait 21.0)
 constexpr int kLeastChunks = kWarps;         // a chunk a warp: 333 keys 7.1 us, with 16 chunks 12.1
 
-// CTAs an SM holds (registers: at most 128 or 168 a thread) and ring stages a warp.  For QT = 4 and
-// D = 128, four CTAs of 128 registers spill and were slower (64 ragged sequences 57 us against 52);
-// three stages of 32 keys were no faster than two.
-constexpr int ctas_per_sm(int D, int QT) { return D == 64 && QT == 4 ? 4 : 3; }
-constexpr int stages(int D) { return 2 * (128 / D); }         // a power of two
+// Ring stages a warp, a power of two: three of 32 keys were no faster than two.
+constexpr int stages(int D) { return 2 * (128 / D); }
 
 struct PagedAttnArgs {
     const float *q;
@@ -312,7 +310,7 @@ __device__ __forceinline__ void join_parts(Part part, int n, int nq, float *s_w,
 }
 
 template <int D, int QT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a)
+__global__ void __launch_bounds__(kThreads, dlp::attn_ctas_per_sm(D, QT)) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a)
 {
     constexpr int NB = D / 32;               // blocks of 32 channels
     constexpr int S = stages(D), CB = dlp::cell_bytes(D), OS = D + 4;
@@ -934,26 +932,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, QT)) paged_attn_kerne
             if (!dla::mbar_wait(&s_full[warp][j & (S - 1)], (uint32_t)(j / S) & 1u)) break;
 }
 
-struct Geometry {
-    size_t counters, parts;                  // bytes
-    size_t total() const { return counters + parts; }
-};
-
-int geometry(int sms, int D, int QT, Geometry *out)
-{
-    const int grid = sms * ctas_per_sm(D, QT);
-    out->counters = ((size_t)grid * 12 + 15) / 16 * 16;
-    out->parts = (size_t)grid * 2 * QT * (D + 2) * 4;
-    return grid;
-}
-
 template <int D, int QT>
 int launch(PagedAttnArgs &a, int sms, int64_t most_chunks, unsigned char *workspace, cudaStream_t st)
 {
-    Geometry geo;
-    const int full = geometry(sms, D, QT, &geo);
+    static_assert(dlp::attn_ctas_per_sm(D, QT) <= dlp::kMostCtasPerSm, "counters of more CTAs");
+    const dlp::AttnLayout layout = dlp::attn_layout(sms, D, QT);
+    const int full = layout.grid;
     a.counters = reinterpret_cast<int *>(workspace);
-    a.parts = reinterpret_cast<float *>(workspace + geo.counters);
+    a.parts = reinterpret_cast<float *>(workspace + layout.counters);
     const int G = a.n_q / a.n_kv;
     const int64_t tiles = dl::ceil_div((int64_t)a.max_rows * G, QT);
     if (tiles * a.n_kv * most_chunks > 0x7fffffff)
@@ -991,9 +977,8 @@ size_t workspace_bytes_for(int sms, int D)
 {
     size_t most = 0;
     for (int QT = 4; QT <= 8; QT *= 2) {
-        Geometry g;
-        geometry(sms, D, QT, &g);
-        if (g.total() > most) most = g.total();
+        const size_t total = dlp::attn_layout(sms, D, QT).total();
+        if (total > most) most = total;
     }
     return most;
 }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged
-from tests.test_paged_gpu import _check, _cuda, _pool, _tables
+from tests.test_paged_gpu import _check, _cuda, _pool, _rope, _tables
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,31 @@ def test_select_from_two_threads(dl):
     assert refused == [0, 0]
     for _, pages, want, _ in runs:
         assert np.array_equal(pages.cpu().numpy(), want)
+
+
+def test_one_workspace_for_all_calls(dl):
+    """Calls of single tokens and of several rows, with heads of 64 and of 128, take turns on one workspace; parts joined
+    in groups among them.  Each gives what it gives on a workspace of its own, and leaves the counters zero."""
+    rng = np.random.default_rng(14)
+    page, n_kv, lens = 16, 2, [5000, 40, 9000]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    calls = []
+    for D, n_q, rows in ((64, 8, 1), (64, 8, 3), (128, 8, 1), (128, 16, 3), (64, 16, 1)):
+        tables, n_pages = _tables(rng, lens, page)
+        kv = dl.PagedKV.empty(n_pages, n_kv, page, D)
+        n = sum(lens)
+        seq = np.repeat(np.arange(3), lens).astype(np.int32)
+        pos = np.concatenate([np.arange(x) for x in lens]).astype(np.int32)
+        gt, gs, gpos, gl = _cuda(tables, seq, pos, np.array(lens, np.int32))
+        x = torch.randn(n, n_kv * D, device="cuda")
+        dl.dl_paged_append(torch.zeros(n, n_kv * D, device="cuda"), x, x, gpos, gt, _rope(dl, 0, 9000, True), kv, n_kv,
+                           row_seq=gs)
+        q = torch.randn(3 * rows, n_q * D, device="cuda")
+        begin = None if rows == 1 else torch.arange(0, 3 * rows + 1, rows, dtype=torch.int32, device="cuda")
+        kw = dict(q=q, kv=kv, tables=gt, seqlen=gl, n_q=n_q, row_begin=begin, max_rows=rows)
+        calls.append((kw, dl.dl_paged_attn(workspace=dl.paged_attn_workspace(n_q, n_kv, D), **kw)))
+    ws = dl.paged_attn_workspace(16, n_kv, 128)
+    for i in [0, 1, 0, 2, 0, 3, 4, 1, 4, 2, 1, 3, 2, 0]:
+        kw, want = calls[i]
+        assert torch.equal(dl.dl_paged_attn(workspace=ws, **kw), want), i
+        assert (ws[:48 * sms] == 0).all()               # three counters for each of up to four CTAs an SM
