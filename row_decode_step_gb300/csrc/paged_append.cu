@@ -14,7 +14,8 @@ namespace dlp {
 
 int check_cache(const char *who, const dl_paged_kv *kv, const dl_block_tables *t, int n_q, bool want_mean)
 {
-    if (!kv || !t || !kv->pool || !t->pages) return dl::fail(DL_E_ARG, "%s: null pointer", who);
+    // (an empty batch may have no address for what it has no elements of)
+    if (!kv || !t || !kv->pool || (!t->pages && t->n_seqs > 0)) return dl::fail(DL_E_ARG, "%s: null pointer", who);
     if (kv->head_dim != 64 && kv->head_dim != 128)
         return dl::fail(DL_E_SHAPE, "%s: head_dim=%d (64 or 128)", who, kv->head_dim);
     if (!page_ok(kv->page)) return dl::fail(DL_E_SHAPE, "%s: page=%d (16, 32, 64, 128 or 256)", who, kv->page);
@@ -508,7 +509,7 @@ int dl_paged_append(const float *q, int64_t q_stride, const float *k, int64_t k_
                     int32_t *status, dl_stream_t stream)
 {
     dl::clear_error();
-    if (!q || !k || !v || !pos || !rope || (!rope->cos_sin && rope->rot_dim > 0))
+    if ((rows != 0 && (!q || !k || !v || !pos)) || !rope || (!rope->cos_sin && rope->rot_dim > 0))
         return dl::fail(DL_E_ARG, "dl_paged_append: null pointer");
     int rc = dlp::check_cache("dl_paged_append", kv, tables, n_q, false);
     if (rc != DL_OK) return rc;

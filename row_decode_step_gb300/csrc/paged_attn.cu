@@ -1006,7 +1006,8 @@ int dl_paged_attn(const float *q, int64_t q_stride, const dl_paged_kv *kv, const
                   void *workspace, size_t workspace_bytes, int32_t *status, dl_stream_t stream)
 {
     dl::clear_error();
-    if (!q || !seqlen || !out || !workspace) return dl::fail(DL_E_ARG, "dl_paged_attn: null pointer");
+    if ((rows != 0 && (!q || !out)) || (!seqlen && tables && tables->n_seqs != 0) || !workspace)
+        return dl::fail(DL_E_ARG, "dl_paged_attn: null pointer");
     int rc = dlp::check_cache("dl_paged_attn", kv, tables, n_q, false);
     if (rc != DL_OK) return rc;
     rc = check_heads("dl_paged_attn", n_q, kv->n_kv, kv->head_dim);

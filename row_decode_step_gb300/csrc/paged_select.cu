@@ -378,7 +378,7 @@ int dl_paged_select(const float *q, int64_t q_stride, const dl_paged_kv *kv, con
                     int32_t *pages, int32_t *status, dl_stream_t stream)
 {
     dl::clear_error();
-    if (!q || !seqlen || !pages) return dl::fail(DL_E_ARG, "dl_paged_select: null pointer");
+    if (rows != 0 && (!q || !seqlen || !pages)) return dl::fail(DL_E_ARG, "dl_paged_select: null pointer");
     int rc = dlp::check_cache("dl_paged_select", kv, tables, n_q, true);
     if (rc != DL_OK) return rc;
     if (rows != tables->n_seqs)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged
-from tests.test_paged_gpu import _check, _cuda, _pool, _rope, _tables
+from tests.test_paged_gpu import THETA, _check, _cuda, _pool, _rope, _tables
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +149,37 @@ def test_one_workspace_for_all_calls(dl):
         kw, want = calls[i]
         assert torch.equal(dl.dl_paged_attn(workspace=ws, **kw), want), i
         assert (ws[:48 * sms] == 0).all()               # three counters for each of up to four CTAs an SM
+
+
+def test_empty_batches(dl):
+    """Steps of no rows, from tensors without elements (whose address is 0), leave everything as it was."""
+    D, page, n_q, n_kv = 64, 16, 4, 2
+    kv = dl.PagedKV.empty(4, n_kv, page, D, means=True)
+    kv.pool.fill_(17)
+    kv.k_mean.fill_(3.0)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    ws, rope = dl.paged_attn_workspace(n_q, n_kv, D), dl.make_rope(THETA, D, 32)
+    status = i32(1)
+    for tables in (i32(0, 3), i32(2, 3)):
+        n = tables.shape[0]
+        for seq in (None, i32(0)):
+            dl.dl_paged_append(f32(0, n_q * D), f32(0, n_kv * D), f32(0, n_kv * D), i32(0), tables, rope, kv, n_q, row_seq=seq,
+                               q_out=f32(0, n_q * D), k_out=f32(0, n_kv * D), v_out=f32(0, n_kv * D), status=status)
+        out = dl.dl_paged_attn(f32(0, n_q * D), kv, tables, i32(n), ws, n_q, lse=f32(0, n_q), row_begin=i32(n + 1), max_rows=2,
+                               status=status)
+        assert out.shape == (0, n_q * D)
+    none = i32(0, 3)
+    assert dl.dl_paged_attn(f32(0, n_q * D), kv, none, i32(0), ws, n_q, status=status).shape == (0, n_q * D)
+    pages = dl.dl_paged_select(f32(0, n_q * D), kv, none, i32(0), n_q, top_k=2, n_sink=1, n_local=1, status=status)
+    assert pages.shape == (0, n_kv, 4)
+    dl.dl_paged_attn(f32(0, n_q * D), kv, none, i32(0), ws, n_q, pages=pages, status=status)
+    rows = torch.full((3, n_q * D), 7.0, device="cuda")        # rows of no sequence
+    out = rows.clone()
+    dl.dl_paged_attn(rows, kv, none, i32(0), ws, n_q, out, row_begin=i32(1), max_rows=2, status=status)
+    assert dl.dl_status_read(status) == 0
+    assert (out == 7.0).all() and (kv.pool == 17).all() and (kv.k_mean == 3.0).all() and (ws == 0).all()
+    # rows whose sequences no table knows are skipped as others outside the tables are
+    dl.dl_paged_append(f32(2, n_q * D), f32(2, n_kv * D), f32(2, n_kv * D), i32(2), none, rope, kv, n_q, row_seq=i32(2),
+                       status=status)
+    assert dl.dl_status_read(status) == dl.DL_STATUS_REGION_RANGE and (kv.pool == 17).all()
