@@ -307,8 +307,9 @@ static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     if (listed < 0) return NULL;
     pages = (const int32_t *)pg.p;
     if (listed) {
-        if (pg.dim != 3 || pg.size[0] != rows || pg.size[1] != h.kv->n_kv || pg.size[2] > INT32_MAX || !dense(&pg)) {
-            PyErr_Format(PyExc_ValueError, "pages must be contiguous [%lld][%d][listed]", (long long)rows, h.kv->n_kv);
+        if (pg.dim != 3 || pg.size[0] != rows || pg.size[1] != h.kv->n_kv || pg.size[2] < 1 ||
+            pg.size[2] > INT32_MAX || !dense(&pg)) {
+            PyErr_Format(PyExc_ValueError, "pages must be contiguous [%lld][%d][>= 1]", (long long)rows, h.kv->n_kv);
             return NULL;
         }
         n_list = (int)pg.size[2];

@@ -183,3 +183,15 @@ def test_empty_batches(dl):
     dl.dl_paged_append(f32(2, n_q * D), f32(2, n_kv * D), f32(2, n_kv * D), i32(2), none, rope, kv, n_q, row_seq=i32(2),
                        status=status)
     assert dl.dl_status_read(status) == dl.DL_STATUS_REGION_RANGE and (kv.pool == 17).all()
+
+
+def test_empty_page_list(dl):
+    """A list without room for a page is refused (its tensor has no address, which would read every page)."""
+    D, page, n_q, n_kv = 64, 16, 4, 2
+    kv = dl.PagedKV.empty(4, n_kv, page, D)
+    kv.pool.zero_()
+    q = torch.zeros(2, n_q * D, device="cuda")
+    tables, lens = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        dl.dl_paged_attn(q, kv, tables, lens, dl.paged_attn_workspace(n_q, n_kv, D), n_q,
+                         pages=torch.zeros(2, n_kv, 0, dtype=torch.int32, device="cuda"))
