@@ -159,6 +159,14 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(*shape, dtype, device, stream=None) -> torch.Tensor:
+    """Memory of the stream the call runs on: what the current stream has freed may still be read there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)

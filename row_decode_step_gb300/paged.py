@@ -2,7 +2,8 @@
 
 Like the rest of the binding this marshals arguments only: dl_paged_append, dl_paged_attn and
 dl_paged_select carry the C names of include/dl.h and take torch tensors.  All tensors of a call
-lie on one device; the call runs on that device's current stream unless `stream` names another.
+lie on one device; the call runs on that device's current stream unless `stream` names another, whose
+memory the results then are that the call makes itself.
 The tensors are checked in csrc/paged_call.c (in Python the checks took longer than a small call).
 """
 from __future__ import annotations
@@ -12,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from . import Rope, _check, dl_paged_kv, lib
+from . import Rope, _check, _empty, dl_paged_kv, lib
 
 _PAGES = (16, 32, 64, 128, 256)
 _native = None
@@ -118,7 +119,7 @@ def dl_paged_attn(q: torch.Tensor, kv: PagedKV, tables: torch.Tensor, seqlen: to
                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of the rows over their sequences' pages (all, or those that `pages` lists)."""
     if out is None:
-        out = torch.empty(q.shape[0], n_q * kv.head_dim, dtype=torch.float32, device=kv.device)
+        out = _empty(q.shape[0], n_q * kv.head_dim, dtype=torch.float32, device=kv.device, stream=stream)
     _call(_calls().attn, kv, stream, q, tables, seqlen, workspace, n_q, out, lse, row_begin, max_rows, pages, status)
     return out
 
@@ -129,6 +130,6 @@ def dl_paged_select(q: torch.Tensor, kv: PagedKV, tables: torch.Tensor, seqlen: 
     """The pages worth reading of every row and KV head (int32 [rows][n_kv][n_sink + top_k + n_local],
     ascending, -1 past them), for dl_paged_attn's `pages`."""
     if pages is None:
-        pages = torch.empty(q.shape[0], kv.n_kv, n_sink + top_k + n_local, dtype=torch.int32, device=kv.device)
+        pages = _empty(q.shape[0], kv.n_kv, n_sink + top_k + n_local, dtype=torch.int32, device=kv.device, stream=stream)
     _call(_calls().select, kv, stream, q, tables, seqlen, n_q, pages, top_k, n_sink, n_local, status)
     return pages

@@ -195,3 +195,33 @@ def test_empty_page_list(dl):
     with pytest.raises(ValueError):
         dl.dl_paged_attn(q, kv, tables, lens, dl.paged_attn_workspace(n_q, n_kv, D), n_q,
                          pages=torch.zeros(2, n_kv, 0, dtype=torch.int32, device="cuda"))
+
+
+def test_results_made_on_the_named_stream(dl):
+    """A result that the call makes itself is memory of the stream it runs on: not a block that the current stream's
+    queued work still reads."""
+    D, page, n_q, n_kv, n = 64, 16, 8, 2, 64
+    rng = np.random.default_rng(4)
+    tables, n_pages = _tables(rng, [page] * n, page)
+    pool, mean = _pool(rng, n_pages, n_kv, page, D)
+    gp, gm, gt = _cuda(pool, mean, tables)
+    kv = dl.PagedKV(gp, page, D, k_mean=gm)
+    q, lens = torch.ones(n, n_q * D, device="cuda"), torch.full((n,), page, dtype=torch.int32, device="cuda")
+    ws, side = dl.paged_attn_workspace(n_q, n_kv, D), torch.cuda.Stream()
+    big = torch.zeros(1 << 28, device="cuda")
+    kw = dict(top_k=61, n_sink=1, n_local=2)
+    calls = (((n, n_q * D), torch.float32, lambda: dl.dl_paged_attn(q, kv, gt, lens, ws, n_q, stream=side)),
+             ((n, n_kv, 64), torch.int32, lambda: dl.dl_paged_select(q, kv, gt, lens, n_q, stream=side, **kw)))
+    for shape, dtype, call in calls:
+        call()                                          # (first launches load code)
+        kept = torch.full(shape, 7, dtype=dtype, device="cuda")
+        seen = torch.zeros_like(kept)
+        torch.cuda.synchronize()
+        for _ in range(20):                             # some milliseconds before the read
+            big.add_(1.0)
+        seen.copy_(kept)
+        del kept
+        got = call()
+        torch.cuda.synchronize()
+        assert (seen == 7).all()
+        assert got.shape == shape
