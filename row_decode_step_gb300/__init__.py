@@ -202,8 +202,8 @@ def dl_q8_pack(blocks: torch.Tensor, n_out: int, n_in: int, stream=None) -> Pack
     if not blocks.is_contiguous() or blocks.numel() != n_out * (n_in // 32) * 34:
         raise ValueError("blocks must be contiguous [n_out][n_in/32][34]")
     qb, db = dl_q8_packed_size(n_out, n_in)
-    qs = torch.empty(qb, dtype=torch.uint8, device=blocks.device)
-    d = torch.empty(db, dtype=torch.uint8, device=blocks.device)
+    qs = _empty(qb, dtype=torch.uint8, device=blocks.device, stream=stream)
+    d = _empty(db, dtype=torch.uint8, device=blocks.device, stream=stream)
     _check(lib().dl_q8_pack(_ptr(blocks), n_out, n_in, _ptr(qs), _ptr(d), _stream(stream)))
     return PackedQ8(qs, d, n_out, n_in)
 
@@ -233,7 +233,7 @@ def dl_f16w_pack(w: torch.Tensor, stream=None) -> PackedF16W:
     if w.dim() != 2 or not w.is_contiguous():
         raise ValueError("w must be a contiguous [n_out][n_in] float16 tensor")
     n_out, n_in = w.shape
-    packed = torch.empty(dl_f16w_packed_size(n_out, n_in), dtype=torch.uint8, device=w.device)
+    packed = _empty(dl_f16w_packed_size(n_out, n_in), dtype=torch.uint8, device=w.device, stream=stream)
     _check(lib().dl_f16w_pack(_ptr(w), n_out, n_in, _ptr(packed), _stream(stream)))
     return PackedF16W(packed, n_out, n_in)
 
@@ -250,7 +250,7 @@ def dl_gemv_q8(W: PackedQ8, x: torch.Tensor, y: Optional[torch.Tensor] = None, s
         raise ValueError("x must be 2-D with unit inner stride")
     rows = x.shape[0]
     if y is None:
-        y = torch.empty(rows, W.n_out, dtype=torch.float32, device=x.device)
+        y = _empty(rows, W.n_out, dtype=torch.float32, device=x.device, stream=stream)
     _dev(y, torch.float32, "y")
     if path == GEMV_PATH_AUTO:
         _check(lib().dl_gemv_q8(ctypes.byref(W.c), _ptr(x), rows, x.stride(0), _ptr(y), y.stride(0),
@@ -269,7 +269,7 @@ def dl_gemv_f16w(W: PackedF16W, x: torch.Tensor, y: Optional[torch.Tensor] = Non
         raise ValueError("x must be 2-D with unit inner stride")
     rows = x.shape[0]
     if y is None:
-        y = torch.empty(rows, W.n_out, dtype=torch.float32, device=x.device)
+        y = _empty(rows, W.n_out, dtype=torch.float32, device=x.device, stream=stream)
     _dev(y, torch.float32, "y")
     if path == GEMV_PATH_AUTO:
         _check(lib().dl_gemv_f16w(ctypes.byref(W.c), _ptr(x), rows, x.stride(0), _ptr(y), y.stride(0),
@@ -559,9 +559,9 @@ def decode_attention(q, kv, seqlen, plan, workspace, out=None, lse=None, status=
     """dl_decode_attn followed by dl_attn_merge; returns (out, lse)."""
     rows = plan.rows
     if out is None:
-        out = torch.empty(rows, plan.n_q * plan.head_dim, dtype=torch.float32, device=q.device)
+        out = _empty(rows, plan.n_q * plan.head_dim, dtype=torch.float32, device=q.device, stream=stream)
     if lse is None:
-        lse = torch.empty(rows, plan.n_q, dtype=torch.float32, device=q.device)
+        lse = _empty(rows, plan.n_q, dtype=torch.float32, device=q.device, stream=stream)
     dl_decode_attn(q, kv, seqlen, plan, workspace, status=status, stream=stream, path=path)
     dl_attn_merge(workspace, plan, seqlen, out, lse, stream=stream)
     return out, lse
