@@ -3,17 +3,21 @@
 The library is plain nvcc output: every csrc/*.cu file becomes an object, the
 objects are linked into row_decode_step_gb300/libdl_gb300.so.  Objects are
 built in parallel and only when their sources changed.  csrc/paged_call.c, the
-CPython side of the paged cache's calls, becomes row_decode_step_gb300/_paged_call.so
-(the host compiler and Python's own header).
+CPython side of the paged cache's calls, becomes row_decode_step_gb300/_paged_call.<ABI
+tag>.so, built for the interpreter that runs this and found by no other.  It takes the host
+compiler and Python's own header; where one is missing the library is built without it, and
+the paged cache's calls from Python say so.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import shlex
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdl_gb300.so")
-CALL = os.path.join(PKG, "_paged_call.so")
+CALL = os.path.join(PKG, "_paged_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -33,6 +37,18 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _call_compiler():
+    """The command that compiles csrc/paged_call.c, less its files; None, with a warning, where it cannot be had."""
+    cc = shlex.split(os.environ.get("CC") or "gcc")
+    header = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    missing = cc[0] if not shutil.which(cc[0]) else header if not os.path.exists(header) else None
+    if missing:
+        warnings.warn("%s is missing: %s is not built, and the paged cache's calls from Python will not run"
+                      % (missing, os.path.basename(CALL)))
+        return None
+    return cc + ["-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", os.path.dirname(header)]
 
 
 def _deps() -> list:
@@ -59,11 +75,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + deps):
             jobs.append([cc] + ARCH + NVCC_FLAGS + ["-c", s, "-o", o])
 
-    call_src = os.path.join(CSRC, "paged_call.c")
+    call_src, call_tmp = os.path.join(CSRC, "paged_call.c"), None
     if force or _stale(CALL, [call_src, os.path.join(INCLUDE, "dl.h")]):
-        tmp_call = CALL + ".tmp.%d" % os.getpid()
-        jobs.append([os.environ.get("CC") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
-                     sysconfig.get_paths()["include"], call_src, "-o", tmp_call])
+        call_cc = _call_compiler()
+        if call_cc:
+            call_tmp = CALL + ".tmp.%d" % os.getpid()
+            jobs.append(call_cc + [call_src, "-o", call_tmp])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -75,8 +92,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
             list(ex.map(run, jobs))
-        if jobs[-1][-1].startswith(CALL):
-            os.replace(jobs[-1][-1], CALL)
+        if call_tmp:
+            os.replace(call_tmp, CALL)
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp.%d" % os.getpid()
         run([cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"])

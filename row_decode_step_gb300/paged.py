@@ -27,8 +27,8 @@ def _calls():
         try:
             from . import _paged_call as m
         except ImportError as e:
-            raise RuntimeError("_paged_call.so is not built (run __graft_entry__.build() or "
-                               "python row_decode_step_gb300/_build.py)") from e
+            raise RuntimeError("_paged_call is not built for this interpreter (run __graft_entry__.build() or python "
+                               "row_decode_step_gb300/_build.py, with a host compiler and Python.h)") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.dl_paged_append, L.dl_paged_attn, L.dl_paged_select)),
                torch.float32, torch.int32, torch.uint8)
         _native = m
