@@ -402,7 +402,9 @@ __global__ void __launch_bounds__(256, MEAN ? 4 : 5) paged_append_kernel(const _
 // Mean keys of the pages that the launch before filled, each by a CTA of 256 threads: a thread takes two
 // channels of a cell, the cells' sums pass through shared memory to be added in their order.  (A page and
 // head by a warp, eight channels a lane, cost 3 to 8 us more: 96 rows 7.2 us instead of 4.6.)  Grid: (sets
-// of `per` rows, KV heads); the rows that wrote a page's last key are found before the wait.
+// of `per` rows, KV heads); the rows that wrote a page's last key are found before the wait: the launch before
+// is this call's store, which lets this one start only after its own wait, so that whatever wrote positions,
+// sequences and tables has finished, and it writes none of them itself.
 template <int D>
 __global__ void __launch_bounds__(256) paged_mean_kernel(const __grid_constant__ AppendArgs a, int per)
 {

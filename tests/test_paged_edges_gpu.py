@@ -225,3 +225,76 @@ def test_results_made_on_the_named_stream(dl):
         torch.cuda.synchronize()
         assert (seen == 7).all()
         assert got.shape == shape
+
+
+@pytest.mark.parametrize("n", [48, 700])
+@pytest.mark.parametrize("with_seq", [True, False])
+def test_append_arguments_of_the_kernel_before(dl, n, with_seq):
+    """Positions, sequences and table entries that the kernel right before the store writes (another store, whose q
+    without rotation carries their bits): the store's two launches must go by them, not by what was there."""
+    D, page, n_kv, cols = 64, 16, 2, 64
+    rng = np.random.default_rng(n)
+    if with_seq:                                        # prompts of a few sequences, pages filled throughout
+        lens = [n - n // 3, n // 3]
+        seq, pos = np.repeat(np.arange(2), lens), np.concatenate([np.arange(x) for x in lens])
+    else:                                               # a row each, half of them filling a page
+        lens = [int(x) for x in rng.integers(1, 60, n)]
+        lens[::2] = [page * int(x) for x in rng.integers(1, 4, len(lens[::2]))]
+        seq, pos = np.arange(n), np.array(lens) - 1
+    tables, n_pages = _tables(rng, lens, page, width=64)
+    pool, mean = _pool(rng, n_pages, n_kv, page, D)
+    k, v = (rng.standard_normal((n, n_kv * D)).astype(np.float32) for _ in range(2))
+    wide = lambda x: np.concatenate([x, np.zeros(-len(x) % cols, x.dtype)]).reshape(-1, cols).astype(np.int32)  # noqa: E731
+    good = dict(pos=wide(pos), seq=wide(seq), tab=tables)
+    bad = dict(pos=wide(rng.choice([-1, page - 1, 1 << 30, 0], n)), seq=wide(rng.choice([-1, 1, 1 << 30, 0], n)),
+               tab=rng.choice([-1, n_pages, 0, 1 << 30], tables.shape).astype(np.int32))
+    # padding where every other argument is still the old one: an early look must not be followed
+    put_src = {(w, i): torch.from_numpy(x[w]).cuda().view(torch.float32) for i, x in enumerate((good, bad)) for w in x}
+    words = {w: torch.zeros_like(put_src[w, 0]) for w in good}
+    m = max(len(x) for x in words.values())
+    other = dl.PagedKV.empty(m, 1, page, D)
+    own, zero = torch.arange(m, dtype=torch.int32, device="cuda").view(m, 1), torch.zeros(m, dtype=torch.int32, device="cuda")
+    kvx, rope = torch.zeros(m, D, device="cuda"), _rope(dl, 0, 4096, False)
+
+    def put(what, i):
+        x = put_src[what, i]
+        c = len(x)
+        dl.dl_paged_append(x, kvx[:c], kvx[:c], zero[:c], own[:c], rope, other, 1, q_out=words[what])
+
+    order = ["pos", "seq", "tab"] if with_seq else ["pos", "tab"]
+    caches = []
+    for _ in order:
+        gp, gm = _cuda(pool, mean)
+        caches.append(dl.PagedKV(gp, page, D, k_mean=gm))
+    gk, gv = _cuda(k, v)
+    gq, status = torch.zeros(n, D * n_kv, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = {w: words[w].view(torch.int32) for w in words}
+
+    def run():
+        for last, kv in zip(order, caches):
+            for w in order:
+                put(w, w == last)
+            put(last, 0)                                # the kernel right before the store
+            dl.dl_paged_append(gq, gk, gv, args["pos"].view(-1)[:n], args["tab"], rope, kv, n_kv,
+                               row_seq=args["seq"].view(-1)[:n] if with_seq else None, status=status)
+
+    want_pool, want_mean = pool.copy(), mean.copy()
+    paged.append(want_pool, want_mean, np.zeros((n, n_kv * D), np.float32), k, v, pos, seq, tables, n_q=n_kv, n_kv=n_kv, D=D,
+                 page=page, rot=0, theta=THETA, neox=False)
+
+    def check():
+        torch.cuda.synchronize()
+        assert dl.dl_status_read(status) == 0
+        for kv in caches:
+            assert np.array_equal(kv.pool.cpu().numpy(), want_pool) and np.array_equal(kv.k_mean.cpu().numpy(), want_mean)
+            kv.pool.copy_(torch.from_numpy(pool))
+            kv.k_mean.copy_(torch.from_numpy(mean))
+
+    run()
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(3):
+        g.replay()
+        check()
