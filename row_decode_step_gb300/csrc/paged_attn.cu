@@ -24,8 +24,8 @@
 // 4-7 the lo terms.  Tiles of 16 queries would decode a key once for both halves, but their 255
 // registers leave two CTAs an SM (24 sequences of 1 to 5 drafted rows 70 us, in tiles of eight 68).
 //
-// Bound by a warp's own chain of instructions (730 for 32 keys, 0.6 a cycle and scheduler): 16 sequences
-// of 32768 keys run at 4.5 TB/s (134 us), with the codes used undecoded (wrong, to see) at 5.3.
+// Bound by a warp's own chain of instructions (740 for 32 keys, 0.6 a cycle and scheduler): 16 sequences
+// of 32768 keys run at 4.5 TB/s (133 us), with the codes used undecoded (wrong, to see) at 5.3.
 #include <cmath>
 
 #include "dl_async.cuh"
@@ -39,8 +39,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 2 * dlp::kCell;       // keys a warp takes at a time
 constexpr int kItemCost = 12;                // an item's queries, join and output, in chunks
 // Items of at most kUncut chunks are not cut: their parts' join would cost more than the balance gains (333
-// keys 7.1 us, cut 10.6; 256 short sequences 20.0 and 21.0; with 40 chunks 19.0, but 64 ragged sequences 52 -> 53
-// and 48 sequences of 1088 chosen keys 22.7 -> 25.0).
+// keys 7.1 us, cut 10.6; 256 short sequences 20.0 and 21.0; with 40 chunks 18.9, but 64 ragged sequences 52.2 ->
+// 53.9 and 48 sequences of 1088 chosen keys 22.8 -> 25.2).
 constexpr int kUncut = 24;
 constexpr int kKept = 512;                   // sequences whose lengths a CTA copies; more are planned after the wait
                                              // (256 short sequences: 20.0 us, after the wait 21.0)
@@ -743,7 +743,8 @@ __global__ void __launch_bounds__(kThreads, dlp::attn_ctas_per_sm(D, QT)) paged_
                                           mraw[1] == -INFINITY ? 0.f : fmaf(mraw[1], cq.y, -kshift));
                 // References as large as this are off by a quarter of an exponent and more, so that the products'
                 // exact differences from them are nobody's weights (past f16 from 2^25 on): here the scores are
-                // rounded first and the largest weight is 1, chunk by chunk.
+                // rounded first and the largest weight is 1, chunk by chunk.  (The exponents pass on from here, which costs
+                // 24 drafted sequences 67.7 -> 68.2 us; computed again below, with a factor for these, 69.8.)
                 const bool far_x = fabsf(nref.x) >= kFar, far_y = fabsf(nref.y) >= kFar;
                 if (far_x) nref.x = __fmul_rn(mraw[0], cq.x);
                 if (far_y) nref.y = __fmul_rn(mraw[1], cq.y);
