@@ -179,8 +179,10 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) paged_select_kernel(
     }
     if (rank == 0)
         for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<int4 *>(hist)[i] = make_int4(0, 0, 0, 0);
-    for (int d = tid; d < D; d += kThreads) {
-        const float *src = a.q + r * a.q_stride + (int64_t)h * G * D + d;
+    static_assert(D <= kThreads, "a channel a thread");
+    bool mine = false;                       // the thread's channel passes 2^100
+    if (tid < D) {
+        const float *src = a.q + r * a.q_stride + (int64_t)h * G * D + tid;
         double s = 0.0;
         for (int g0 = 0; g0 < G; g0 += 8) {          // (eight loads in flight)
             float v[8];
@@ -190,10 +192,25 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) paged_select_kernel(
             for (int g = 0; g < 8; ++g)
                 if (g0 + g < G) s += (double)v[g];
         }
-        s_hi[d] = (float)s;
-        s_lo[d] = isfinite(s) ? (float)(s - (double)s_hi[d]) : 0.f;
+        float hi = (float)s;
+        mine = fabsf(hi) >= 0x1p100f;
+        if (mine) {
+            s *= 0x1p-64;
+            hi = (float)s;
+        }
+        s_hi[tid] = hi;
+        s_lo[tid] = isfinite(hi) ? (float)(s - (double)hi) : 0.f;
     }
-    __syncthreads();
+    // from 2^100 on sums, products or their sums might pass f32 where the score does not: they are taken 2^-64
+    // as large, and the scores, rounded, brought back (1 x 131072 keys 0.3 us more)
+    const bool large = __syncthreads_or(mine);
+    if (large) {
+        if (tid < D && !mine) {
+            s_hi[tid] *= 0x1p-64f;
+            s_lo[tid] *= 0x1p-64f;
+        }
+        __syncthreads();
+    }
     // (the first CTA of the cluster runs: its shared memory may be written)
     if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     float2 qh[E / 2], ql[E / 2];
@@ -246,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) paged_select_kernel(
         const int c = c0 + (gl >> 1) * step;
         if ((gl & 1) == 0 && c < nc) {
             float score = isfinite(s1) ? s1 + e1 : s1;       // (an infinite term leaves NaN in e1)
+            if (large) score *= 0x1p64f;
             const int page = b4 ? b2 ? phys[3] : phys[2] : b2 ? phys[1] : phys[0];
             if (page < 0 || page >= a.n_pages) {
                 score = NAN;

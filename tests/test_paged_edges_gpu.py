@@ -298,3 +298,25 @@ def test_append_arguments_of_the_kernel_before(dl, n, with_seq):
     for _ in range(3):
         g.replay()
         check()
+
+
+@pytest.mark.parametrize("qscale", [1e10, 1e20, 1e30, 1e36, 6e37])
+@pytest.mark.parametrize("D,n_q,n_kv", [(128, 16, 2), (64, 6, 3)])
+def test_select_large_queries(dl, D, n_q, n_kv, qscale):
+    """Finite queries whose sums, products or scores pass f32 on the way are ranked as 64 bits rounded to f32 rank them:
+    scores past f32 are infinite and tie, the others count; pages of zeros and of small means are among them."""
+    rng = np.random.default_rng(int(np.log10(qscale)))
+    page, n = 16, 1500
+    lens, tables = [n * page] * 2, np.arange(2 * n, dtype=np.int32).reshape(2, n)
+    mean = (rng.standard_normal((2 * n, n_kv, D)) * 10.0 ** rng.integers(-4, 2, (2 * n, n_kv, 1))).astype(np.float16)
+    mean[rng.integers(0, 2 * n, 60), :, ::2] = 0.0
+    mean[rng.integers(0, 2 * n, 60)] = 0.0
+    q = (rng.uniform(-5, 5, (2, n_q * D)) * qscale).astype(np.float32)
+    q[1, :n_q * D // 2] = np.abs(q[1, :n_q * D // 2])   # the group's sum passes f32 at the largest size
+    assert np.isfinite(q).all()
+    kw = dict(n_q=n_q, n_kv=n_kv, D=D, page=page, top_k=400, sink=1, local=2)
+    want = paged.select(q, mean, tables, lens, **kw)
+    gq, gm, gt, gl = _cuda(q, mean, tables, np.array(lens, np.int32))
+    kv = dl.PagedKV(dl.PagedKV.empty(2 * n, n_kv, page, D).pool, page, D, k_mean=gm)
+    got = dl.dl_paged_select(gq, kv, gt, gl, n_q, top_k=400, n_sink=1, n_local=2)
+    assert np.array_equal(got.cpu().numpy(), want)
