@@ -11,9 +11,9 @@
 // to the first CTA's shared memory, which selects: the take-th largest by three histograms of 11, 11
 // and 10 bits, then one scan.
 //
-// One long sequence is bound by latencies (131072 keys, 2048 pages: 9.0 us; the scores 3, the threshold 2,
+// One long sequence is bound by latencies (131072 keys, 2048 pages: 9.2 us; the scores 3, the threshold 2,
 // the list 1.3, the rest start and end); many by the scores' instructions, 11 packed ones to two channels
-// besides the conversion: 32 sequences of up to 512 pages 16.4 us, the longest's CTA last.  Eight lanes a
+// besides the conversion: 32 sequences of up to 512 pages 16.8 us, the longest's CTA last.  Eight lanes a
 // page: sixteen (fewer registers, more warps) spend more on the sums over lanes (4 us more).
 #include <cmath>
 
